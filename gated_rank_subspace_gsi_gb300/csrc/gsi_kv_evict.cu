@@ -206,7 +206,11 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(EvictArgs a) {
 
 // Sixteen codes as fp16, and back: times 2^k (exact, or below half a code's step)
 // and rounded to nearest even.  int8: 1536 + v has v's two's complement in the low
-// byte of an fp16, whose step is 1 there.
+// byte of an fp16, whose step is 1 there.  k is the old scale's exponent less the
+// new one's.  No value of a block is above Q times its new scale, so a code that is
+// not zero has 2^k <= Q / code: k is at most 6 for int8 (least code 1) and 17 for
+// e4m3 (2^-9), where 2^k is no fp16 number beyond 2^15.
+constexpr int kMostUp = 17, kFp16Up = 15;
 template <int FMT>
 __device__ __forceinline__ void codes16_f16(const uint4& w, uint32_t (&f)[8]) {
   codes_f16<FMT>(w.x, f[0], f[1]);
@@ -320,8 +324,19 @@ __global__ void __launch_bounds__(kMoveThreads, D == 256 ? 4 : D == 128 ? 5 : 6)
     for (int i = 0; i < kPer; ++i) {
       uint32_t f[8];
       codes16_f16<FMT>(v[i], f);
-      // 2^(old - new exponent): at most 2^8 for codes that are not zero
-      const __half2 by = __float2half2_rn(fminf(s_scale[kv][(tid + i * kHalf) / kV] * inv, 256.f));
+      // (beyond the most only for rows of zeros)
+      const float up = fminf(s_scale[kv][(tid + i * kHalf) / kV] * inv, float(1 << kMostUp));
+      const float low = fminf(up, float(1 << kFp16Up));
+      const __half2 by = __float2half2_rn(low);
+      if (FMT == kE4m3) {
+        // what is beyond 2^15 (1 but for codes of at most 2^-7) as a factor of its own
+        const __half2 rest = __float2half2_rn(up > low ? up * (1.f / (1 << kFp16Up)) : 1.f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&f[e]), rest);
+          f[e] = *reinterpret_cast<const uint32_t*>(&x);
+        }
+      }
       out[tid + i * kHalf] = make_uint4(f16_codes<FMT>(f[0], f[1], by), f16_codes<FMT>(f[2], f[3], by),
                                         f16_codes<FMT>(f[4], f[5], by), f16_codes<FMT>(f[6], f[7], by));
     }

@@ -1,0 +1,101 @@
+"""The 8-bit key/value cache where sizes differ most: rows beside much larger ones.
+Against plain 64-bit arithmetic (kv_reference.py), as in test_gpu_kv.py.
+"""
+import pytest
+import torch
+
+from kv_reference import read_cache
+from test_gpu_kv import Pair
+
+pytestmark = pytest.mark.gpu
+
+
+def append(p, counts, edit):
+    """Rows of each sequence, edited by edit(k or v, on the CPU); into both caches."""
+    (_, k, v), start = p.rows(counts)
+    for x in (k, v):
+        edit(x[0])
+        x[1].copy_(x[0])
+    p.c.append(k[1], v[1], start, p.len, max(counts))
+    p.len += torch.tensor(counts, dtype=torch.int32, device="cuda")
+    first = 0
+    for b, r in enumerate(counts):
+        p.ref.append(b, k[0][first:first + r], v[0][first:first + r])
+        first += r
+
+
+def scores(p, of):
+    """The score of every token held: of(b, h, n) gives a head's."""
+    for b, n in enumerate(p.len.tolist()):
+        pg = p.c.page_table[b, :-(-n // 64)].long()
+        for h in range(p.heads):
+            x = torch.zeros(len(pg) * 64)
+            x[:n] = of(b, h, n)
+            p.c.score[pg, h] = x.view(-1, 64).cuda()
+    p.ref.score = read_cache(p.c, p.len.tolist())[2]
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("large", [10, 13, 16, 18])
+@pytest.mark.parametrize("stays", [False, True])
+def test_evict_rows_that_leave_a_much_larger_one(gsi, fmt, dim, large, stays):
+    """One row of each page is 2^large times the others and sets their scale.  It is
+    evicted, or lands in another block than some of them; a page of zeros among them."""
+    p = Pair(gsi, 2, 2, 1, dim, fmt, max_pages=8, spare=5, seed=large + dim)
+    counts = [320, 300]
+
+    def at(page, h):
+        return 64 * page + (11 * page + 29 * h + 7) % 64
+
+    def edit(x):
+        for first in (0, 320):
+            x[first + 64:first + 128] = 0
+            for h in range(2):
+                for page in range(5):
+                    if first + at(page, h) < 620:
+                        row = x[first + at(page, h), h * dim:(h + 1) * dim]
+                        row.copy_(torch.randn(dim, generator=p.gen) * 2.0 ** large)
+
+    append(p, counts, edit)
+    p.check_cache()
+
+    def of(b, h, n):
+        s = torch.rand(n, generator=p.gen)
+        for page in range(-(-n // 64)):
+            if at(page, h) < n:
+                s[at(page, h)] = 2.0 if stays else -1.0
+        return s
+
+    scores(p, of)
+    for budget, recent in ((256, 0), (192, 5), (130, 60)):
+        p.c.evict(p.len, budget, recent, p.spare)
+        for b in range(2):
+            p.ref.evict(b, budget, recent)
+        p.check_cache(0.0)
+    assert p.c.status() == 0
+    p.c.close()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_evict_least_codes(gsi, fmt, dim):
+    """Rows of a page's few least codes, alone in their new block: its scale is finer
+    by the greatest factor that there is (2^17 for e4m3, whose least code is 2^-9)."""
+    low = 1.0 if fmt == "int8" else 2.0 ** -9
+    for few in (1, 2, 3, 4, 7):
+        p = Pair(gsi, 1, 1, 1, dim, fmt, max_pages=4, spare=2, seed=few)
+
+        def edit(x):
+            x.copy_(torch.randint(-few, few + 1, x.shape, generator=p.gen) * low)
+            x[::2, 3] = few * low
+            x[5, 9] = x[64 + 60, 0] = 127.0 if fmt == "int8" else 448.0
+
+        append(p, [128], edit)
+        scores(p, lambda b, h, n: torch.tensor([-1.0 if t in (5, 124) or t % 2 else 1.0 for t in range(n)]))
+        p.c.evict(p.len, 64, 0, p.spare)
+        p.ref.evict(0, 64, 0)
+        # the even rows but 124, and of the others the first: neither 5 nor 124
+        assert p.ref.k[0][0].abs().max() <= few * low
+        p.check_cache(0.0)
+        p.c.close()
