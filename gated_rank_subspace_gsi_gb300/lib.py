@@ -513,6 +513,20 @@ def _raw(stream) -> int:
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """torch.empty of the stream that a call is queued on.  The caching allocator
+    gives a block out again in the order of the stream that it was allocated
+    under; under another one the block could still be in use by earlier work of
+    that stream, or serve later work of it while the call runs."""
+    import torch
+    if stream is None or _raw(stream) == _current_stream():
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_raw(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def gsi_kv_append(kv, k, v, row_start, length, max_rows: int, stream=None):
     """Append the packed new rows k, v (rows x heads * D, fp32 or bf16, row
     slices allowed) to the cache; row_start (seqs + 1) and length (seqs: tokens
@@ -626,16 +640,18 @@ class KVCache:
 
     def attention(self, q, row_start, length, max_rows: int, scale=None, out=None, lse=None,
                   accumulate: bool = False, stream=None):
+        """An out that is not given is allocated under the call's stream, as torch
+        would there: work of other streams waits for the call before it reads it."""
         self._ints(row_start, self.seqs + 1, "row_start")
         self._ints(length, self.seqs, "length")
         if q.shape[1] != self.q_heads * self.head_dim:
             raise ValueError("q must be rows x q_heads * head_dim")
         if out is None:
             import torch
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            out = _empty(q.shape, torch.bfloat16, q.device, stream)
         if accumulate and lse is None:
             import torch
-            lse = torch.empty((q.shape[0], self.q_heads), dtype=torch.float32, device=q.device)
+            lse = _empty((q.shape[0], self.q_heads), torch.float32, q.device, stream)
         if lse is not None and lse.numel() != q.shape[0] * self.q_heads:
             raise ValueError("lse must be rows x q_heads")
         scale = self.head_dim ** -0.5 if scale is None else scale
