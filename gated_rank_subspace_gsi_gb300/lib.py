@@ -197,6 +197,26 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _raw(stream) -> int:
+    if stream is None:
+        return _current_stream()
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _empty(shape, dtype, device, stream):
+    """torch.empty of the stream that a call is queued on.  The caching allocator
+    gives a block out again in the order of the stream that it was allocated
+    under; under another one the block could still be in use by earlier work of
+    that stream, or serve later work of it while the call runs."""
+    import torch
+    if stream is None or _raw(stream) == _current_stream():
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_raw(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _check(st: int, what: str):
     if st != GSI_OK:
         raise GsiError(st, what)
@@ -345,10 +365,10 @@ class GatedLinear:
             gsi_reserve(self.h, max_T)
 
     def forward(self, x, y=None, gate=None, rho=None, stream=None):
-        import torch
         T = x.shape[0]
         if y is None:
-            y = torch.empty((T, self.d_out), dtype=torch.float32, device=x.device)
+            import torch
+            y = _empty((T, self.d_out), torch.float32, x.device, stream)
         gsi_forward(self.h, x, y, gate, rho, stream)
         return y
 
@@ -505,26 +525,6 @@ def _kv_rows(t, what: str):
     if dt is None or not t.is_cuda:
         raise TypeError(f"{what} must be an fp32 or bf16 CUDA tensor")
     return t.data_ptr(), (stride[0] if shape[0] > 1 else shape[1]), dt
-
-
-def _raw(stream) -> int:
-    if stream is None:
-        return _current_stream()
-    return stream if isinstance(stream, int) else stream.cuda_stream
-
-
-def _empty(shape, dtype, device, stream):
-    """torch.empty of the stream that a call is queued on.  The caching allocator
-    gives a block out again in the order of the stream that it was allocated
-    under; under another one the block could still be in use by earlier work of
-    that stream, or serve later work of it while the call runs."""
-    import torch
-    if stream is None or _raw(stream) == _current_stream():
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_raw(stream), device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def gsi_kv_append(kv, k, v, row_start, length, max_rows: int, stream=None):

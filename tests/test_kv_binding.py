@@ -1,4 +1,4 @@
-"""The key/value cache's Python binding, with fakes in CUDA's place (CPU)."""
+"""The Python binding with fakes in CUDA's place (CPU): mostly the key/value cache."""
 import contextlib
 
 import pytest
@@ -57,3 +57,12 @@ def test_tensors_made_for_a_call_are_of_its_stream(cuda, stream, accumulate):
     assert cuda["launched"] == [want]
     assert cuda["allocated"] == [want] * (2 if accumulate else 1)
     assert cuda["current"] == 11
+
+
+@pytest.mark.parametrize("stream", [None, 11, 22, FakeStream(33)])
+def test_an_output_of_a_gated_linear_is_of_its_stream(cuda, monkeypatch, stream):
+    monkeypatch.setattr(lib, "gsi_forward", lambda h, x, y, gate, rho, s: cuda["launched"].append(lib._raw(s)))
+    layer = object.__new__(lib.GatedLinear)
+    layer.h, layer.d_out = None, 8
+    layer(torch.zeros((2, 4)), stream=stream)
+    assert cuda["allocated"] == cuda["launched"] == [11 if stream is None else lib._raw(stream)]
