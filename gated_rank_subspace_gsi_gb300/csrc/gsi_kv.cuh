@@ -39,6 +39,15 @@ __device__ __forceinline__ int page_of(const KvView& c, int b, int blk) {
   return p;
 }
 
+// 16 bytes that are read once, without a place in L1.  Not by the read-only path
+// (ld.global.nc): the kernels that fill the pages may still run when this one starts.
+__device__ __forceinline__ uint4 ld_once_v4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
 // Exponent of the least power of two, at least 2^kScaleMin, with
 // top <= Q 2^e.  With top = m 2^x (0.5 <= m < 1): Q = 127 = (127 / 128) 2^7,
 // Q = 448 = 0.875 2^9.

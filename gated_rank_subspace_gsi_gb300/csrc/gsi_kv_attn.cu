@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(32 * weight_warps<D>(), D == 256 ? 1 : 2) weig
           const int row = t0 % kPage + 16 * i + g;  // and 8 further
           if (blk < whole) {
             const uint8_t* src = a.c.codes[0] + (ph * kPage + row) * D + 64 * c + 16 * t;
-            const uint4 x = ld_stream_v4(src), y = ld_stream_v4(src + 8 * D);
+            const uint4 x = ld_once_v4(src), y = ld_once_v4(src + 8 * D);
             const uint32_t wx[4] = {x.x, x.y, x.z, x.w}, wy[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {

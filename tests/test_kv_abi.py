@@ -138,3 +138,19 @@ def test_host_tensors_are_refused(gsi):
         with pytest.raises(TypeError):
             call()
     c.close()
+
+
+def test_kernels_read_no_buffer_as_constant():
+    """Under programmatic dependent launch a kernel of the cache may start while earlier
+    ones of the stream still write the pages: none reads through the read-only path
+    (ld.global.nc, __ldg, what __restrict__ lets the compiler use), whose lines must not
+    change while the kernel lives."""
+    import os
+    import re
+    from gated_rank_subspace_gsi_gb300 import build
+    names = [n for n in os.listdir(build.CSRC) if n.startswith("gsi_kv")]
+    assert len(names) >= 8
+    for n in names:
+        with open(os.path.join(build.CSRC, n)) as f:
+            code = re.sub(r"//[^\n]*", "", f.read())
+        assert not re.search(r"ld_stream_v4|__ldg\b|__restrict__|global\.nc", code), n
