@@ -11,6 +11,22 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Exponents f of V's scales lie in [-80, 122], and sums are kept relative to the
+// maximum m of s + f (logit and exponent).  Where scales of one row's blocks are far
+// apart, 2^f weighs more than fp32 holds although the divisor, a sum of 2^s, does not:
+// - to a larger maximum, sums are brought by two factors of 2^(d / 2), and a divisor
+//   takes them one by one (weighted sums may vanish, they are too small to count);
+// - a scale below 2^-kScaleSpan of the largest before it in the share is taken as
+//   that, so that 2^(s + f - m) is in range wherever 2^s counts.  What the block's
+//   values gain is below 2^-98 of the largest value.
+constexpr int kScaleSpan = 100;
+__device__ __forceinline__ float ex2_half(float d) { return ex2(0.5f * d); }
+// V's scale (bits of a power of two) as it is used; top: the largest so far.
+__device__ __forceinline__ int clip_scale(int bits, int& top) {
+  top = max(top, bits);
+  return max(bits, top - (kScaleSpan << 23));
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);

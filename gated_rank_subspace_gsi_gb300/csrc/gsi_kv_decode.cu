@@ -313,9 +313,9 @@ struct Warp {
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const float r = m[n][c] == -INFINITY ? 0.f : ex2(m[n][c] - mx[n][c]);
+          const float hr = m[n][c] == -INFINITY ? 0.f : ex2_half(m[n][c] - mx[n][c]), r = hr * hr;
           m[n][c] = mx[n][c];
-          l[n][c] *= r;
+          l[n][c] = l[n][c] * hr * hr;
 #pragma unroll
           for (int i = 0; i < kSteps; ++i) {
             o[i][n][c] *= r;
@@ -645,6 +645,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     // what the computing cursor needs of the units in the ring: lane s has
     // stage s's
     float r_ks = 1.f, r_vs = 1.f;
+    int vs_top = 0;  // the largest of V's scales of the head so far
     int r_kind = 2;  // 0: codes, 1: tail, 2: nothing (its page is out of range)
     auto fetch = [&]() {
       if (fu >= u1) return;
@@ -687,9 +688,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
         }
       }
       const float sk = __shfl_sync(0xFFFFFFFFu, ks, pb - fb0), sv = __shfl_sync(0xFFFFFFFFu, vs, pb - fb0);
+      if (fblk == 0) vs_top = 0;
+      const int vs_bits = pg < 0 ? 0 : clip_scale(__float_as_int(sv), vs_top);
       if (lane == s) {
         r_ks = sk;
-        r_vs = sv;
+        r_vs = __int_as_float(vs_bits);
         r_kind = pg < 0 ? 2 : in_pages ? 0 : 1;
       }
       if (fblk == 0 || fu == u0) {
@@ -859,7 +862,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     float top = -INFINITY;
     for (int k = s_start[gi]; k < s_start[gi + 1]; ++k) top = fmaxf(top, s_ml[s_list[k]][row][0]);
     const float m = s_ml[s_list[at]][row][0];
-    s_f[at][row] = m == -INFINITY ? 0.f : ex2(m - top);
+    const float hf = m == -INFINITY ? 0.f : ex2_half(m - top);
+    s_f[at][row] = hf * hf;
+    s_ml[s_list[at]][row][1] = s_ml[s_list[at]][row][1] * hf * hf;
     if (at == s_start[gi]) s_top[gi][row] = top;
   }
   __syncthreads();
@@ -879,14 +884,14 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     if (far)
       o = __ldcg(reinterpret_cast<const float4*>(
                      p.piece + ((size_t(blockIdx.x) * kWarps + last / 2) * R + row) * D) + d);
-    float l = far ? s_ml[last][row][1] * s_f[k1 - 1][row] : 0.f;
+    float l = far ? s_ml[last][row][1] : 0.f;
     const float fl = far ? s_f[k1 - 1][row] : 0.f;
     o.x *= fl; o.y *= fl; o.z *= fl; o.w *= fl;
     for (int k = k0; k < k1 - far; ++k) {
       const int pc = s_list[k];
       const float f = s_f[k][row];
       const float4 v = reinterpret_cast<const float4*>(all + size_t(pc / 2) * S * Sh::kBytes)[row * kD4 + d];
-      l = fmaf(s_ml[pc][row][1], f, l);
+      l += s_ml[pc][row][1];
       o.x = fmaf(v.x, f, o.x);
       o.y = fmaf(v.y, f, o.y);
       o.z = fmaf(v.z, f, o.z);
@@ -951,14 +956,14 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
       float mx = top;
 #pragma unroll
       for (int e = 0; e < kN; ++e) mx = fmaxf(mx, ml[e].x);
-      const float f0 = top == -INFINITY ? 0.f : ex2(top - mx);
-      l *= f0;
+      const float h0 = top == -INFINITY ? 0.f : ex2_half(top - mx), f0 = h0 * h0;
+      l = l * h0 * h0;
       o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
       top = mx;
 #pragma unroll
       for (int e = 0; e < kN; ++e) {
-        const float f = ml[e].x == -INFINITY ? 0.f : ex2(ml[e].x - mx);
-        l = fmaf(ml[e].y, f, l);
+        const float hf = ml[e].x == -INFINITY ? 0.f : ex2_half(ml[e].x - mx), f = hf * hf;
+        l = fmaf(ml[e].y * hf, hf, l);
         o.x = fmaf(v[e].x, f, o.x);
         o.y = fmaf(v[e].y, f, o.y);
         o.z = fmaf(v[e].z, f, o.z);

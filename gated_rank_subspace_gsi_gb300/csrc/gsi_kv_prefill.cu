@@ -353,9 +353,9 @@ __global__ void __launch_bounds__(Shape<D, HL>::kThreads, 1)
       top = top == -INFINITY ? -INFINITY : fmaf(top, k, f);
       const bool grow = top > m + kGrow || (m == -INFINITY && top > -INFINITY);
       if (__any_sync(0xFFFFFFFFu, grow)) {
-        const float scale = !grow ? 1.f : m == -INFINITY ? 0.f : ex2(m - top);
+        const float hs = ex2_half(grow ? m - top : 0.f), scale = hs * hs;  // (0 where m is -inf)
         if (grow) m = top;
-        l *= scale;
+        l = l * hs * hs;
         if (j > 0) {
           ok = wait_often(&o_done[tile][(j - 1) & 1], ((j - 1) >> 1) & 1, status, &s_abort);
           ok = __all_sync(0xFFFFFFFFu, ok);
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(Shape<D, HL>::kThreads, 1)
   } else if (warp == kSoft + kConv) {
     // ---- the rings of codes ---------------------------------------------------
     // pages and scales of 32 blocks at a time, one per lane
-    int page = -1, j = 0;
+    int page = -1, j = 0, vs_top = 0;
     float2 sc = make_float2(0.f, 1.f);
     bool ok = true;
     for (; ok && j < pages; ++j) {
@@ -616,8 +616,9 @@ __global__ void __launch_bounds__(Shape<D, HL>::kThreads, 1)
       const bool codes = pg >= 0 && j < whole;
       const int line = (pg * H + h) * (D == 64 ? kPage / 2 : kPage);
       // (the scales of page j - 16 are out of use: the rings are that short)
+      const int vs = clip_scale(__shfl_sync(0xFFFFFFFFu, __float_as_int(sc.y), j % 32), vs_top);
       if (lane == j % 32) {
-        s_scale[j % kScales] = sc;
+        s_scale[j % kScales] = make_float2(sc.x, __int_as_float(vs));
         mbar_arrive_cta(&sc_full[j % kScales]);
       }
       __syncwarp();

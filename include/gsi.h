@@ -500,7 +500,8 @@ gsi_status_t gsi_kv_append(gsi_kv_t kv, const void *k, int64_t ldk, const void *
  *        and lse
  * q is carried as two fp16 parts where weights or lse are asked for, else as
  * one (11 bits); p as one; products accumulate in fp32, and maxima, sums and
- * the weights are fp32. */
+ * the weights are fp32.  Values may differ in size by any factor; one below
+ * 2^-100 of the largest may count as that much. */
 gsi_status_t gsi_kv_attention(gsi_kv_t kv, const void *q, int64_t ldq, gsi_dtype_t dtype,
                               const int32_t *row_start, int64_t rows, int64_t max_rows,
                               const int32_t *len, float scale, void *out, int64_t ldo,

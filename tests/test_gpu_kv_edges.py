@@ -99,3 +99,29 @@ def test_evict_least_codes(gsi, fmt, dim):
         assert p.ref.k[0][0].abs().max() <= few * low
         p.check_cache(0.0)
         p.c.close()
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("rows,group", [(1, 1), (1, 8), (3, 4), (40, 2), (150, 1)])
+@pytest.mark.parametrize("lse", [True, False])
+def test_attention_over_values_of_all_sizes(gsi, dim, rows, group, lse):
+    """Blocks whose values differ by up to 2^170: a row's divisor counts them alike,
+    whichever comes first, in one share of a head or in several."""
+    for sizes in ((90, None, 0, 85), (None, 90), (-70, 40, -70, 89, 0, -70), (0, None, None, 90, None, 3)):
+        p = Pair(gsi, 2, 1, group, dim, "int8", max_pages=16, seed=rows + dim)
+        n = 64 * len(sizes)
+
+        def edit(x):
+            for first in (0, n):
+                for j, size in enumerate(sizes):
+                    x[first + 64 * j:first + 64 * j + 64] *= 0.0 if size is None else 2.0 ** size
+
+        (_, k, v), start = p.rows([n, n])
+        edit(v[0])
+        v[1].copy_(v[0])
+        p.c.append(k[1], v[1], start, p.len, n)
+        p.len += n
+        for b in range(2):
+            p.ref.append(b, k[0][b * n:b * n + n], v[0][b * n:b * n + n])
+        p.check_out([rows, 1], lse=lse, accumulate=lse)
+        assert p.c.status() == 0
+        p.c.close()
