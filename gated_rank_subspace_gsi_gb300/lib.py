@@ -530,20 +530,24 @@ def _kv_rows(t, what: str):
 def gsi_kv_append(kv, k, v, row_start, length, max_rows: int, stream=None):
     """Append the packed new rows k, v (rows x heads * D, fp32 or bf16, row
     slices allowed) to the cache; row_start (seqs + 1) and length (seqs: tokens
-    held before the call): int32 CUDA tensors."""
+    held before the call): int32 CUDA tensors.  max_rows: a bound of the new rows
+    of a sequence; one above the rows of the call will do."""
     kp, ldk, dt = _kv_rows(k, "k")
     vp, ldv, dtv = _kv_rows(v, "v")
     if dtv != dt or k.shape != v.shape:
         raise ValueError("k and v differ in shape or type")
-    _check(_load().gsi_kv_append(kv, kp, ldk, vp, ldv, dt, row_start.data_ptr(), k.shape[0],
-                                 max_rows, length.data_ptr(), _raw(stream)), "gsi_kv_append")
+    rows = k.shape[0]
+    _check(_load().gsi_kv_append(kv, kp, ldk, vp, ldv, dt, row_start.data_ptr(), rows,
+                                 min(max_rows, rows), length.data_ptr(), _raw(stream)),
+           "gsi_kv_append")
 
 
 def gsi_kv_attention(kv, q, row_start, length, max_rows: int, scale: float, out, lse=None,
                      accumulate: bool = False, stream=None):
     """Attention of the new rows q (rows x q_heads * D, fp32 or bf16) over the
     cache, after gsi_kv_append of the same rows with the same length; out: bf16.
-    accumulate adds each token's weight to the cache's score (needs lse)."""
+    accumulate adds each token's weight to the cache's score (needs lse).
+    max_rows as for gsi_kv_append; rows of a sequence beyond it are not computed."""
     qp, ldq, dt = _kv_rows(q, "q")
     op, ldo, dto = _kv_rows(out, "out")
     if dto != GSI_BF16 or out.shape != q.shape:
@@ -552,8 +556,9 @@ def gsi_kv_attention(kv, q, row_start, length, max_rows: int, scale: float, out,
         import torch
         if not (lse.dtype == torch.float32 and lse.is_cuda and lse.is_contiguous()):
             raise TypeError("lse must be a contiguous fp32 CUDA tensor")
-    _check(_load().gsi_kv_attention(kv, qp, ldq, dt, row_start.data_ptr(), q.shape[0], max_rows,
-                                    length.data_ptr(), scale, op, ldo,
+    rows = q.shape[0]
+    _check(_load().gsi_kv_attention(kv, qp, ldq, dt, row_start.data_ptr(), rows,
+                                    min(max_rows, rows), length.data_ptr(), scale, op, ldo,
                                     None if lse is None else lse.data_ptr(), 1 if accumulate else 0,
                                     _raw(stream)), "gsi_kv_attention")
 

@@ -472,8 +472,9 @@ gsi_status_t gsi_kv_create(const gsi_kv_buffers_t *buffers, gsi_kv_t *out);
  *   k, v     rows x (heads * D), fp32 or bf16 (dtype), rows ldk / ldv elements
  *            apart (>= heads * D): slices of a fused qkv output will do.
  *            16-byte aligned, row strides multiples of 16 bytes
- *   max_rows the largest number of new rows of any sequence (host): sizes the
- *            launch; more rows are still appended, with less parallelism
+ *   max_rows the largest number of new rows of any sequence (host), 0 .. rows:
+ *            sizes the launch; more rows are still appended, with less
+ *            parallelism
  *   len      seqs int32 (device): tokens held before the call
  * The pages that the new tokens need must be in page_table.  A sequence that
  * runs out of pages drops the rest (GSI_ERR_PAGE).  With score, the new
@@ -489,8 +490,8 @@ gsi_status_t gsi_kv_append(gsi_kv_t kv, const void *k, int64_t ldk, const void *
  *   out = sum_j p_j v_j, p = softmax_j(scale q . k_j)
  * Query head a reads key/value head a / (q_heads / heads).
  *   q    rows x (q_heads * D), fp32 or bf16, ldq elements apart; alignment as k
- *   max_rows  at least the largest number of new rows of any sequence: rows
- *        beyond it are not computed (GSI_ERR_PAGE)
+ *   max_rows  at least the largest number of new rows of any sequence, at most
+ *        `rows`: a sequence's rows beyond it are not computed (GSI_ERR_PAGE)
  *   out  rows x (q_heads * D) bf16, ldo elements apart; alignment as k.  It is
  *        the next gated linear's x
  *   lse  rows x q_heads fp32 or NULL: ln sum_j exp(scale q . k_j), -inf for a

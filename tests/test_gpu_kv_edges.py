@@ -4,7 +4,7 @@ Against plain 64-bit arithmetic (kv_reference.py), as in test_gpu_kv.py.
 import pytest
 import torch
 
-from kv_reference import read_cache
+from kv_reference import out_bound, read_cache
 from test_gpu_kv import Pair
 
 pytestmark = pytest.mark.gpu
@@ -125,3 +125,25 @@ def test_attention_over_values_of_all_sizes(gsi, dim, rows, group, lse):
         p.check_out([rows, 1], lse=lse, accumulate=lse)
         assert p.c.status() == 0
         p.c.close()
+
+
+def test_a_bound_of_rows_above_the_rows_of_a_call(gsi):
+    """A fixed bound, say of drafted tokens, with fewer new rows in all, and with none."""
+    p = Pair(gsi, 3, 2, 2, 64, "int8", seed=23)
+    p.step([70, 1, 130])
+    for counts in ([1, 0, 2], [0, 1, 0], [0, 0, 0]):
+        (q, k, v), start = p.rows(counts)
+        p.c.append(k[1], v[1], start, p.len, 5)
+        out = p.c.attention(q[1], start, p.len, 5, accumulate=True)
+        p.len += torch.tensor(counts, dtype=torch.int32, device="cuda")
+        first = 0
+        for b, r in enumerate(counts):
+            if r:
+                rows = slice(first, first + r)
+                p.ref.append(b, k[0][rows], v[0][rows])
+                ro, _, mag, absv = p.ref.attend(b, q[0][rows], 64 ** -0.5)
+                assert ((out[rows].cpu().double() - ro).abs() <= out_bound(ro, mag, absv)).all()
+            first += r
+        p.check_cache()
+    assert p.c.status() == 0
+    p.c.close()
