@@ -189,6 +189,19 @@ def _current_stream() -> int:
     return _raw_stream()
 
 
+_device_index = None
+
+
+def _current_device() -> int:
+    """The current CUDA device's number."""
+    global _device_index
+    if _device_index is None:
+        import torch
+        torch.cuda.init()
+        _device_index = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _device_index()
+
+
 def _stream(stream):
     if stream is None:
         return ctypes.c_void_p(_current_stream())
@@ -588,7 +601,8 @@ class KVCache:
     "e4m3".  buffers: a dict of the tensors below, or None to allocate them
     (page_table then starts as -1: no page).  score=True allocates the
     accumulated weights that eviction goes by.  Lengths are the caller's: int32
-    CUDA tensors of seqs entries.
+    CUDA tensors of seqs entries.  The cache is of the current device, which has
+    to be current in its calls as well, and so are their tensors.
     """
 
     PAGE = 64
@@ -620,6 +634,10 @@ class KVCache:
             if t is None or tuple(t.shape) != shape or t.dtype != dt or not t.is_contiguous() \
                     or not t.is_cuda:
                 raise TypeError(f"{n} must be a contiguous CUDA tensor {shape} of {dt}")
+        self._device = _current_device()
+        for n in shapes:
+            if buffers.get(n) is not None and buffers[n].get_device() != self._device:
+                raise ValueError(f"{n} is not of the current device, cuda:{self._device}")
         self.buffers = dict(buffers)
         for n in shapes:
             setattr(self, n, buffers.get(n))
@@ -633,10 +651,21 @@ class KVCache:
         self.kv = gsi_kv_create(b)
 
     def _ints(self, t, n: int, what: str):
-        if not (t.dtype == self._int and t.is_cuda and t.numel() == n and t.is_contiguous()):
-            raise TypeError(f"{what} must be a contiguous int32 CUDA tensor of {n} entries")
+        if not (t.dtype == self._int and t.get_device() == self._device and t.numel() == n
+                and t.is_contiguous()):
+            raise TypeError(f"{what} must be a contiguous int32 tensor of {n} entries on "
+                            f"cuda:{self._device}")
+
+    def _elsewhere(self):
+        """What is raised where the current device or a tensor is not the cache's."""
+        if _current_device() != self._device:
+            raise ValueError(f"cuda:{self._device}, the cache's device, is not the current one")
+        raise TypeError(f"a tensor of the call is not on cuda:{self._device}")
 
     def append(self, k, v, row_start, length, max_rows: int, stream=None):
+        dev = self._device
+        if _current_device() != dev or k.get_device() != dev or v.get_device() != dev:
+            self._elsewhere()
         self._ints(row_start, self.seqs + 1, "row_start")
         self._ints(length, self.seqs, "length")
         if k.shape[1] != self.heads * self.head_dim:
@@ -647,6 +676,11 @@ class KVCache:
                   accumulate: bool = False, stream=None):
         """An out that is not given is allocated under the call's stream, as torch
         would there: work of other streams waits for the call before it reads it."""
+        dev = self._device
+        if _current_device() != dev or q.get_device() != dev or \
+                (out is not None and out.get_device() != dev) or \
+                (lse is not None and lse.get_device() != dev):
+            self._elsewhere()
         self._ints(row_start, self.seqs + 1, "row_start")
         self._ints(length, self.seqs, "length")
         if q.shape[1] != self.q_heads * self.head_dim:
@@ -666,6 +700,8 @@ class KVCache:
 
     def evict(self, length, budget: int, recent: int, spare_table, length_out=None, stream=None):
         length_out = length if length_out is None else length_out
+        if _current_device() != self._device:
+            self._elsewhere()
         self._ints(length, self.seqs, "length")
         self._ints(length_out, self.seqs, "length_out")
         self._ints(spare_table, self.page_table.numel(), "spare_table")

@@ -444,7 +444,8 @@ int gsi_refine_rank1_launch_count(int64_t n, int64_t d, int64_t k,
  * heads to a head; seqs <= 65535, heads <= 4096;
  * pages * heads * 64 < 2^31 (else GSI_ERR_UNSUPPORTED_SHAPE).  All calls are
  * asynchronous on `stream`, allocate nothing, never synchronise and may be
- * captured in a CUDA graph; calls on one handle must be ordered on the GPU. */
+ * captured in a CUDA graph; calls on one handle must be ordered on the GPU.
+ * The device that was current at gsi_kv_create is current in all calls. */
 typedef struct gsi_kv *gsi_kv_t;
 
 typedef enum { GSI_KV_INT8 = 0, GSI_KV_E4M3 = 1 } gsi_kv_format_t;
