@@ -1,11 +1,12 @@
-"""The 8-bit key/value cache where sizes differ most: rows beside much larger ones.
-Against plain 64-bit arithmetic (kv_reference.py), as in test_gpu_kv.py.
+"""The 8-bit key/value cache where sizes differ most: rows beside much larger ones,
+many sequences, long ones.  Against plain 64-bit arithmetic (kv_reference.py), as in
+test_gpu_kv.py.
 """
 import pytest
 import torch
 
 from kv_reference import out_bound, read_cache
-from test_gpu_kv import Pair
+from test_gpu_kv import Pair, score_bound
 
 pytestmark = pytest.mark.gpu
 
@@ -145,5 +146,42 @@ def test_a_bound_of_rows_above_the_rows_of_a_call(gsi):
                 assert ((out[rows].cpu().double() - ro).abs() <= out_bound(ro, mag, absv)).all()
             first += r
         p.check_cache()
+    assert p.c.status() == 0
+    p.c.close()
+
+
+@pytest.mark.parametrize("seqs,heads,group,dim,rows", [(33, 2, 1, 64, 1), (100, 1, 4, 128, 3), (100, 2, 3, 256, 2),
+                                                       (1100, 2, 1, 64, 1), (1100, 1, 5, 64, 2)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_attention_of_few_rows_of_many_sequences(gsi, seqs, heads, group, dim, rows, accumulate):
+    """More sequences than a warp has lanes, and than shared memory counts at once;
+    runs of sequences without new rows over their edges."""
+    p = Pair(gsi, seqs, heads, group, dim, "e4m3", max_pages=3, seed=seqs + dim)
+    first = torch.randint(0, 140, (seqs,), generator=p.gen).tolist()
+    first[0], first[seqs - 1] = 0, 129
+    p.step(first, lse=False)
+    mag, sums = 0.0, 0
+    for gap in ((30, 66), (1, 32), (seqs - 80, seqs - 1), (seqs, seqs)):
+        counts = torch.randint(0, rows + 1, (seqs,), generator=p.gen).tolist()
+        counts[0] = counts[seqs - 1] = rows
+        for b in range(max(gap[0], 1), min(gap[1], seqs - 1)):
+            counts[b] = 0
+        mag = max(mag, p.check_out(counts, accumulate=accumulate, lse=accumulate))
+        sums += rows * group
+    assert p.c.status() == 0
+    p.check_cache(score_bound(mag, sums) if accumulate else None)
+    p.c.close()
+
+
+@pytest.mark.parametrize("tokens,budget,recent", [(46000, 1000, 100), (46000, 45500, 200), (262400, 20000, 64)])
+def test_evict_from_long_sequences(gsi, tokens, budget, recent):
+    """More scores, and more pages, than the selection keeps in shared memory."""
+    own, spare = -(-tokens // 64), -(-budget // 64)
+    p = Pair(gsi, 1, 1, 1, 64, "e4m3", max_pages=own, spare=spare, seed=budget)
+    append(p, [tokens], lambda x: None)
+    scores(p, lambda b, h, n: torch.floor(300 * torch.rand(n, generator=p.gen) ** 3))
+    p.c.evict(p.len, budget, recent, p.spare)
+    p.ref.evict(0, budget, recent)
+    p.check_cache(0.0)
     assert p.c.status() == 0
     p.c.close()
