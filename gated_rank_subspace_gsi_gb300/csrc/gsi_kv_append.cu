@@ -124,9 +124,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
 template <int FMT, int D>
 gsi_status_t launch(const gsi_kv* kv, const AppendArgs& a, int64_t max_rows, cudaStream_t s) {
   const dim3 grid(unsigned(1 + max_rows / kPage), unsigned(2 * a.c.heads), unsigned(a.c.seqs));
-  // A single new row keeps few threads busy but when it closes a block: small
-  // CTAs, all resident at once (one row of 128 sequences, 8 heads of 128, K and V:
-  // 5.5 us, with 256 threads 6.7).
+  // One or two new rows keep few threads busy but when they close a block: small
+  // CTAs, all resident at once.  128 sequences, 8 heads of 128, K and V, with small
+  // CTAs and with 256 threads: one row 5.5 and 6.8 us, two 6.3 and 7.0, three 6.3 and
+  // 7.2, five 8.3 and 7.9, sixteen 26 and 17; one sequence, 16 heads of 256: one row
+  // and two 2.1 either way, five 2.4 and 2.2.
   constexpr int kFew = D == 256 ? 128 : 64;
   const cudaError_t e = max_rows <= 2 ? launch_pdl(append_kernel<FMT, D, kFew>, grid, dim3(kFew), 0, s, a)
                                       : launch_pdl(append_kernel<FMT, D, 256>, grid, dim3(256), 0, s, a);

@@ -8,12 +8,15 @@
 // have to be as exact as fp32's: their errors are not averaged out where one row
 // weighs most).  Rows in order: the sums do not depend on timing.  Bound by the
 // warp-level MMAs (4 D flops a row and token for the two parts).  Measured: 2000
-// rows over 4049 tokens, 16 heads of 256: 550 us, their pipe busy 74% on the
-// fullest SM; a thread per token in fp32 took 2.2 ms.
+// rows over 4049 tokens, 16 heads of 256: 542 us (beside 187 of the attention with
+// both parts of q), their pipe busy 74% on the fullest SM, 47% on average; a thread
+// per token in fp32 took 2.2 ms.
 //
 // Few heads with many rows would leave most SMs idle: the rows are then shared by
 // CTAs, whose sums a second launch adds in order (3 sequences of 958 to 1210 rows,
-// one head of 256, 7 query heads: 136 us with the attention, unshared 977).
+// one head of 256, 7 query heads: 136 us with the attention, with neither pass shared
+// 1125).  Blocks are counted over max_pages: a cache with far more room than tokens
+// launches CTAs that find nothing to do, and shares no rows.
 #include <algorithm>
 
 #include "gsi_kv.cuh"

@@ -22,8 +22,8 @@
 // share by the last of them to arrive.
 //
 // Measured, one token a sequence: 16 sequences of 1000 to 16001 tokens, 8 heads
-// of 128, 4 query heads to each: 56 us, 5.0 TB/s (74% of a copy); two of 100003
-// and 131071, 8 query heads: 87 us, 5.5 TB/s; one of 2047, 16 heads of 256: 12.2
+// of 128, 4 query heads to each: 56 us, 5.0 TB/s (75% of a copy); two of 100003
+// and 131071, 8 query heads: 86 us, 5.5 TB/s; one of 2047, 16 heads of 256: 12.4
 // us, of which about 10 are a chain that does not depend on the bytes (share of
 // the units, page, codes, join of the warps, arrival, join of the CTAs).  Five
 // rows of 4 sequences of 4000 to 9000, 8 heads of 128, 2 query heads: 30 us.

@@ -14,7 +14,8 @@
 // (length, pages, scores, three digits, kept rows) and then of a block (row,
 // scale and codes, maximum, codes).  Measured: one sequence of 2303 tokens cut
 // to 2048, 16 heads of 256: 21 us; 16 of 3900 to 12001 cut to 4001, 8 heads of
-// 128: 77 us, 3.3 TB/s, the selection a third of it.
+// 128: 79 us, 3.2 TB/s, the selection a third of it; one of 106105 cut to 1000, 2
+// heads of 128: 250 us, nearly all of it two CTAs' selection.
 #include "gsi_kv.cuh"
 #include "gsi_kv_codes.cuh"
 
@@ -237,11 +238,13 @@ __device__ __forceinline__ uint32_t f16_codes(uint32_t lo, uint32_t hi, __half2 
 
 // One new block of a head: K by the first half of the CTA, V by the second.  A
 // block whose rows all come from pages, and which stays in pages, is moved in
-// fp16 (codes of both formats are exact there, 2.5 instructions a code); one with
-// rows from or for the tail in fp32.  CTAs on an SM count for more than registers:
-// at D = 256 four of them, with a few spills, take 79 us for 16 sequences cut to
-// 4001 tokens where three take 83; at D = 128 five take 83 where eight, with
-// spills, take 89 and four 88.
+// fp16 (codes of both formats are exact there, about 3 instructions a code); one with
+// rows from or for the tail in fp32.  CTAs on an SM count for more than registers.
+// Evictions of 16 sequences of 3900 to 12001 tokens to 4001, 8 heads, selection and
+// all: at D = 256 four, with a few spills, 127 us (e4m3) and 130 (int8), three 125 and
+// 132, five 179 and 167 (one sequence of 16 heads, 2303 to 2048: four 21, three 24,
+// five 25); at D = 128 five 82, four 87, eight, with spills, 97; at D = 64 six 63,
+// four 64.
 template <int FMT, int D>
 __global__ void __launch_bounds__(kMoveThreads, D == 256 ? 4 : D == 128 ? 5 : 6) move_kernel(EvictArgs a) {
   constexpr int kHalf = kMoveThreads / 2;

@@ -20,15 +20,15 @@
 // j.  O stays in TMEM; it is rescaled only when a row's maximum has grown by
 // more than 4 (a factor of 16), which P's range allows for.
 //
-// Measured: 2000 rows over 2049 tokens and themselves, 16 heads of 256: 126 us,
-// 790 TFLOP/s (40% of the bf16 rate measured for a large product; the tensor pipe is
-// busy 41% of the time, issue slots 52%: softmax and conversion pace it); four
+// Measured: 2000 rows over 2049 tokens and themselves, 16 heads of 256: 129 us,
+// 775 TFLOP/s (40% of the bf16 rate measured for a large product; the tensor pipe is
+// busy 40% of the time, issue slots 51%: softmax and conversion pace it); four
 // prompts of 301 to 1023, 12 heads of 64: 22 us.
 //
 // Few rows of few heads over a long cache would leave most SMs idle: the pages
 // are then split over CTAs, and a second launch joins their outputs (fp32, each
 // over its own sum) by the logarithms of their sums.  130 rows over 16000 tokens,
-// 16 heads of 256: 90 us, unsplit 270.
+// 16 heads of 256: 90 us, unsplit 279.
 #include <cuda.h>
 
 #include <algorithm>

@@ -560,7 +560,8 @@ def gsi_kv_attention(kv, q, row_start, length, max_rows: int, scale: float, out,
     """Attention of the new rows q (rows x q_heads * D, fp32 or bf16) over the
     cache, after gsi_kv_append of the same rows with the same length; out: bf16.
     accumulate adds each token's weight to the cache's score (needs lse).
-    max_rows as for gsi_kv_append; rows of a sequence beyond it are not computed."""
+    max_rows as for gsi_kv_append; rows of a sequence beyond it are not computed.
+    fp32 queries count with 11 bits, and with 21 where an lse is given."""
     qp, ldq, dt = _kv_rows(q, "q")
     op, ldo, dto = _kv_rows(out, "out")
     if dto != GSI_BF16 or out.shape != q.shape:

@@ -501,7 +501,9 @@ gsi_status_t gsi_kv_append(gsi_kv_t kv, const void *k, int64_t ldk, const void *
  *        new rows and the query heads of its head.  Needs the buffers' score
  *        and lse
  * q is carried as two fp16 parts where weights or lse are asked for, else as
- * one (11 bits); p as one; products accumulate in fp32, and maxima, sums and
+ * one of 11 bits: bf16 rows are exact in that, and with fp32 rows a logit is off
+ * by up to 2^-11 |scale| sum_d |q_d k_d| (which an lse takes down to 2^-21).  p is
+ * one fp16 part; products accumulate in fp32, and maxima, sums and
  * the weights are fp32.  Values may differ in size by any factor; one below
  * 2^-100 of the largest may count as that much. */
 gsi_status_t gsi_kv_attention(gsi_kv_t kv, const void *q, int64_t ldq, gsi_dtype_t dtype,
